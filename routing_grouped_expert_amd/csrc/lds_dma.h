@@ -39,15 +39,15 @@ __device__ __forceinline__ u32x4 uniform(const u32x4& v) {
 //
 // The scalar operands may come from v_readfirstlane, and a load must be five
 // wait states behind the vector instruction that wrote a scalar register it
-// reads; the compiler does not look into the asm, so the wait stands there: the
-// move to m0 is one state, s_nop 3 four (s_nop 0 would do for m0 alone).
+// reads; the compiler does not look into the asm, so the wait stands there
+// (s_nop 4 is five states, one of which m0 needs too). m0, where the load takes
+// its LDS address from, is an operand: the compiler sets it and knows.
 __device__ __forceinline__ void dma16(const u32x4& rs, uint32_t lds, uint32_t voff, uint32_t soff) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 3\n\t"
+      "s_nop 4\n\t"
       "buffer_load_dwordx4 %1, %2, %3 offen lds"
       :
-      : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(uniform(rs)), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+      : "{m0}"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(uniform(rs)), "s"(__builtin_amdgcn_readfirstlane((int)soff))
       : "memory");
 }
 
@@ -55,22 +55,20 @@ __device__ __forceinline__ void dma16(const u32x4& rs, uint32_t lds, uint32_t vo
 // hold for others).
 __device__ __forceinline__ void dma16_once(const u32x4& rs, uint32_t lds, uint32_t voff, uint32_t soff) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 3\n\t"
+      "s_nop 4\n\t"
       "buffer_load_dwordx4 %1, %2, %3 offen nt lds"
       :
-      : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(uniform(rs)), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+      : "{m0}"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(uniform(rs)), "s"(__builtin_amdgcn_readfirstlane((int)soff))
       : "memory");
 }
 
 // The same with 4 bytes a lane.
 __device__ __forceinline__ void dma4(const u32x4& rs, uint32_t lds, uint32_t voff) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 3\n\t"
+      "s_nop 4\n\t"
       "buffer_load_dword %1, %2, 0 offen lds"
       :
-      : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(uniform(rs))
+      : "{m0}"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(uniform(rs))
       : "memory");
 }
 

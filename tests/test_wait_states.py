@@ -5,7 +5,7 @@ A vector memory instruction that reads a scalar register (a buffer's
 descriptor, a scalar offset or base) must come at least five wait states behind
 the vector instruction that wrote the register: every instruction between is
 one, s_nop n is n + 1. The compiler keeps this for its own instructions, not for
-those written as asm."""
+those written as asm. And what asm writes without saying so."""
 import glob
 import os
 import re
@@ -132,3 +132,19 @@ def test_the_check_finds_them():
     assert not run(("v_readfirstlane_b32", "s8, v2", None), load)
     assert run(load, nop(0), first, ("s_cbranch_scc1", "65000", 0))
     assert not run(load, first, nop(3), ("s_cbranch_scc1", "65000", 0))
+
+
+def test_asm_names_m0():
+    """asm that writes m0 says so (as a clobber, or by taking it as an operand
+    that the compiler sets): the compiler may keep an index or an LDS address
+    there."""
+    src = os.path.join(moe.PKG, "csrc")
+    found = 0
+    for f in sorted(os.listdir(src)):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(src, f)).read())
+        for m in re.finditer(r"\basm volatile\s*\((.*?)\);", text, re.S):
+            code, _, rest = m[1].partition("\n      :")
+            found += "m0" in m[1]
+            if re.search(r"\bm0\s*,", code):
+                assert '"m0"' in rest, f"{f}: {code.strip()}"
+    assert found >= 4
