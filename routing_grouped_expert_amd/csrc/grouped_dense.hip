@@ -256,32 +256,27 @@ struct Loads {
                                         int wave, int lane) {
     const int k0 = c.kc * K, KK = c.contraction(a);
     const bool q_in = k0 + piece<K>(lane % LPR, lane / LPR) * 8 < KK;  // rows layout
+    uint32_t at_a[AN], at_b[BN];
 #pragma unroll
     for (int j = 0; j < AN; ++j) {
       const int kk = 2 * (AN * wave + j) + (lane >> 5);  // columns layout
-      uint32_t v = va[j], so = 0;
-      if (A_ROWS) {
-        so = (uint32_t)k0 * 2u;
-        if (!q_in) v = kPastEnd;
-      } else if (P == Product::kDx) {
-        so = (uint32_t)k0 * (uint32_t)a.K * 2u;
-        if (k0 + kk >= KK) v = kPastEnd;
-      } else {
-        v = src[j] == kPastEnd || v == kPastEnd ? kPastEnd : src[j] + v;
-      }
-      dma16(ra, slot + (AN * wave + j) * 1024u, v, so);
+      const uint32_t v = va[j];
+      if (A_ROWS)
+        at_a[j] = q_in ? v : kPastEnd;
+      else if (P == Product::kDx)
+        at_a[j] = k0 + kk < KK ? v : kPastEnd;
+      else
+        at_a[j] = src[j] == kPastEnd || v == kPastEnd ? kPastEnd : src[j] + v;
     }
+    dma16_run<false>(ra, slot + AN * wave * 1024u, at_a,
+                     A_ROWS ? (uint32_t)k0 * 2u : P == Product::kDx ? (uint32_t)k0 * (uint32_t)a.K * 2u : 0u);
 #pragma unroll
     for (int j = 0; j < BN; ++j) {
-      uint32_t v = vb[j], so = (uint32_t)k0 * 2u;
-      if (B_ROWS) {
-        if (!q_in) v = kPastEnd;
-      } else {
-        so = (uint32_t)k0 * (uint32_t)a.M * 2u;
-        if (k0 + 2 * (BN * wave + j) + (lane >> 5) >= KK) v = kPastEnd;
-      }
-      dma16(rb, slot + Shape<TC>::A + (BN * wave + j) * 1024u, v, so);
+      const bool in = B_ROWS ? q_in : k0 + 2 * (BN * wave + j) + (lane >> 5) < KK;
+      at_b[j] = in ? vb[j] : kPastEnd;
     }
+    dma16_run<false>(rb, slot + Shape<TC>::A + BN * wave * 1024u, at_b,
+                     (uint32_t)k0 * 2u * (B_ROWS ? 1u : (uint32_t)a.M));
   }
 };
 

@@ -142,18 +142,21 @@ __global__ __launch_bounds__(WAVES * kWave) void skinny_kernel(MxArgs a, int mos
   auto load = [&]() {
     const uint32_t mine = lds0 + sl * SLOT + wave * WAVE_BYTES, xto = lds0 + sl * SLOT + WAVES * WAVE_BYTES;
     const uint32_t aw = cl.kc * 128u, ax = cl.kc * (uint32_t)F::XROW;
+    uint32_t w_at[4], x_at[XN];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int i = 8 * j + (lane >> 3);
       const bool in = (int)aw + place<8>(lane & 7, i) * 16 < wbytes;
-      dma16_once(rw, mine + j * 1024u, in ? vw[j] : kPastEnd, aw);
+      w_at[j] = in ? vw[j] : kPastEnd;
     }
+    dma16_run<true>(rw, mine, w_at, aw);
 #pragma unroll
     for (int j = 0; j < XN; ++j) {
       const int i = (XN * wave + j) * XROWS + lane / F::XP;
       const bool in = (int)ax + place<F::XP>(lane % F::XP, i) * 16 < xbytes;
-      dma16(rx, xto + (XN * wave + j) * 1024u, in ? vx[j] : kPastEnd, ax);
+      x_at[j] = in ? vx[j] : kPastEnd;
     }
+    dma16_run<false>(rx, xto + XN * wave * 1024u, x_at, ax);
     if (MX && cl.kc % S_RUN == 0) {
       const uint32_t to = scales0 + run_l * 2048;
       dma16_bytes(rws, a.ws + (size_t)cl.expert * a.M * KB, ws_end, to,

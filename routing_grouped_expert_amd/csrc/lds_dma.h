@@ -51,18 +51,47 @@ __device__ __forceinline__ void dma16(const u32x4& rs, uint32_t lds, uint32_t vo
       : "memory");
 }
 
-// The same for data that is read once (it does not displace what the caches
-// hold for others).
-__device__ __forceinline__ void dma16_once(const u32x4& rs, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile(
-      "s_nop 4\n\t"
-      "buffer_load_dwordx4 %1, %2, %3 offen nt lds"
-      :
-      : "{m0}"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(uniform(rs)), "s"(__builtin_amdgcn_readfirstlane((int)soff))
-      : "memory");
+// Two of them behind one wait, the second to the 1 KB that follows. ONCE: for
+// data that is read once (it does not displace what the caches hold for others).
+template <bool ONCE>
+__device__ __forceinline__ void dma16_two(const u32x4& rs, uint32_t lds, uint32_t v0, uint32_t v1,
+                                          uint32_t soff) {
+  int m = __builtin_amdgcn_readfirstlane((int)lds);
+  const u32x4 r = uniform(rs);
+  const int s = __builtin_amdgcn_readfirstlane((int)soff);
+  if (ONCE)
+    asm volatile(
+        "s_nop 4\n\t"
+        "buffer_load_dwordx4 %1, %3, %4 offen nt lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %2, %3, %4 offen nt lds"
+        : "+{m0}"(m)
+        : "v"(v0), "v"(v1), "s"(r), "s"(s)
+        : "memory", "scc");
+  else
+    asm volatile(
+        "s_nop 4\n\t"
+        "buffer_load_dwordx4 %1, %3, %4 offen lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %2, %3, %4 offen lds"
+        : "+{m0}"(m)
+        : "v"(v0), "v"(v1), "s"(r), "s"(s)
+        : "memory", "scc");
 }
 
-// The same with 4 bytes a lane.
+// N loads to consecutive KB from `lds` on.
+template <bool ONCE, int N>
+__device__ __forceinline__ void dma16_run(const u32x4& rs, uint32_t lds, const uint32_t (&voff)[N],
+                                          uint32_t soff) {
+  static_assert(N % 2 == 0 || !ONCE, "single loads keep what they read");
+#pragma unroll
+  for (int j = 0; j + 1 < N; j += 2) dma16_two<ONCE>(rs, lds + j * 1024u, voff[j], voff[j + 1], soff);
+  if (N % 2) dma16(rs, lds + (N - 1) * 1024u, voff[N - 1], soff);
+}
+
+// One load with 4 bytes a lane.
 __device__ __forceinline__ void dma4(const u32x4& rs, uint32_t lds, uint32_t voff) {
   asm volatile(
       "s_nop 4\n\t"

@@ -80,12 +80,14 @@ struct Rows {
   // The pieces of stage kc into LDS at `to`; pieces past the row's end as zeros.
   __device__ __forceinline__ void issue(int kc, int row_bytes, uint32_t to, int wave, int lane) {
     const int at = kc * ROW;
+    uint32_t from[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int i = (N * wave + j) * (64 / LPR) + lane / LPR;
       const bool in = at + piece_of<ROW>(lane % LPR, i) * 16 < row_bytes;
-      dma16(rs, to + (N * wave + j) * 1024u, in ? v[j] : kPastEnd, (uint32_t)at);
+      from[j] = in ? v[j] : kPastEnd;
     }
+    dma16_run<false>(rs, to + N * wave * 1024u, from, (uint32_t)at);
   }
 };
 

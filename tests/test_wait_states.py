@@ -135,16 +135,17 @@ def test_the_check_finds_them():
 
 
 def test_asm_names_m0():
-    """asm that writes m0 says so (as a clobber, or by taking it as an operand
-    that the compiler sets): the compiler may keep an index or an LDS address
+    """asm that writes m0 says so (as a clobber or as an operand that it
+    changes): the compiler may keep an index or an LDS address
     there."""
     src = os.path.join(moe.PKG, "csrc")
     found = 0
     for f in sorted(os.listdir(src)):
         text = re.sub(r"//[^\n]*", "", open(os.path.join(src, f)).read())
         for m in re.finditer(r"\basm volatile\s*\((.*?)\);", text, re.S):
-            code, _, rest = m[1].partition("\n      :")
+            code, *rest = re.split(r"\n\s*:", m[1])
+            rest = "".join(rest)
             found += "m0" in m[1]
             if re.search(r"\bm0\s*,", code):
-                assert '"m0"' in rest, f"{f}: {code.strip()}"
+                assert '"m0"' in rest or '"+{m0}"' in rest, f"{f}: {code.strip()}"
     assert found >= 4
