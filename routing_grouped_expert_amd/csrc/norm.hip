@@ -47,8 +47,17 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
   return s;
 }
 
+// 1 / sqrt(sum / H + eps), rounded once: the instruction's value s (off by a
+// step or two), then s + s / 2 (1 - a s^2) with 1 - a s^2 from the exact a s.
+// (A root and a division, each rounded, were up to 0.97 of a step off, against
+// 0.5, in the same time. The sum's own rounding is larger: of 88 million MXFP8
+// codes 59 differ from those of 64 bits, 57 before.) Zero, infinite and NaN sums
+// give the instruction's infinity, 0 and NaN.
 __device__ __forceinline__ float rstd_of(float sum, int H, float eps) {
-  return 1.0f / sqrtf(sum / (float)H + eps);
+  const float a = sum / (float)H + eps, s = rsqrtf(a);
+  const float as = a * s, low = fmaf(a, s, -as);
+  const float e = fmaf(-low, s, fmaf(-as, s, 1.0f));
+  return a > 0.0f && s > 0.0f ? fmaf(0.5f * s, e, s) : s;
 }
 
 // One row per NT threads (NT 64: four rows a block). H <= NT * 8 * CH, a

@@ -232,3 +232,31 @@ def test_more_rows_than_a_launch_holds(T, H):
     ref = plain.norm(host(h[-3:]).view(np.uint16), None, host(w).astype(np.float64), EPS)[2]
     plain.check(bf16_to_f64(host(y[-3:]).view(np.uint16)), ref,
                 np.abs(ref) * (plain.BF16 + 2 * rel(H)) + 1e-40, "last rows")
+
+
+@pytest.mark.parametrize("H", [8, 1])
+def test_reciprocal_root_is_rounded_once(H):
+    """The row's 1 / sqrt(mean + eps) is the nearest fp32 value but for cases that
+    lie within 2^-6 of a step of the middle between two (a first value off by at most
+    4 steps, corrected once: the correction's own roundings and its second order are
+    below that). Seen in dweight: with one row h = (1, 0, ..) and dy = 1 it is the
+    root itself. The mean is 1 / H and eps a multiple of 2^-24 that makes their sum
+    exact."""
+    t = torch()
+    n = 256
+    rng = np.random.default_rng(H)
+    eps = rng.integers(1, 1 << 20, n) * 2.0 ** -24 * (1 if H == 8 else 2)
+    h = np.zeros((1, H), np.uint16)
+    h[0, 0] = 0x3F80
+    one = np.full((1, H), 0x3F80, np.uint16)
+    dg, dx = buf((n, H), 4), buf((1, H), 2)
+    ws = t.empty(max(256, moe.rms_norm_backward_workspace_size(1, H)), dtype=t.uint8, device="cuda:0")
+    gh, gdy, gw = dev(h), dev(one), dev(np.ones(H, np.float32))
+    note(f"reciprocal root H={H}")
+    for i in range(n):
+        moe.rms_norm_backward(gdy, gh, gw, float(eps[i]), dx, dg[i], ws)
+    sync()
+    got = host(dg)[:, 0].astype(np.float64)
+    s = 1 / np.sqrt(1 / H + eps)
+    step = 2.0 ** (np.floor(np.log2(s)) - 23)
+    assert (np.abs(got - s) <= (0.5 + 2.0 ** -6) * step).all(), (np.abs(got - s) / step).max()
