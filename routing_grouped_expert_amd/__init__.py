@@ -362,20 +362,24 @@ def _out_fp32(t, name):
     return t.element_size() == 4
 
 
-def _here(*tensors):
+def _here(*tensors, whole=(), ws=None):
     """Raise ValueError unless the tensors are on the current device, the one
     the call launches on, and hold none of the types that have the size of an
-    operand's without being it (integers are taken as the bits they are)."""
+    operand's without being it: `tensors` are values and codes (16- and 8-bit
+    integers are taken as the bits they are; 4 bytes are fp32), `whole` offsets
+    and selections (int32), ws a workspace of any type."""
     torch = _torch()
     d = torch.cuda.current_device()
     others = _other_types or _set_other_types(torch)
-    for t in tensors:
-        if t is None:
-            continue
-        if t.get_device() != d:
+    for t in tensors + whole + (ws,):
+        if t is not None and t.get_device() != d:
             raise ValueError(f"a tensor is on device {t.get_device()}, the current one is {d}")
-        if t.dtype in others:
+    for t in tensors:
+        if t is not None and t.dtype in others:
             raise ValueError(f"{t.dtype} is no type of an operand here")
+    for t in whole:
+        if t is not None and t.dtype is not torch.int32:
+            raise ValueError(f"{t.dtype} is no type of offsets or selections, they are int32")
 
 
 _other_types = None
@@ -383,7 +387,8 @@ _other_types = None
 
 def _set_other_types(torch):
     global _other_types
-    names = ("float16", "float8_e4m3fnuz", "float8_e5m2", "float8_e5m2fnuz")
+    names = ("float16", "float8_e4m3fnuz", "float8_e5m2", "float8_e5m2fnuz", "bool", "int32",
+             "uint32", "complex32")
     _other_types = frozenset(getattr(torch, n) for n in names if hasattr(torch, n))
     return _other_types
 
@@ -409,7 +414,7 @@ def grouped_matmul(x, expert_offsets, w, y, permuted_rows=None, k=1, stream=None
     _need(w, "w", (L, M, K), 2)
     f32 = _out_fp32(y, "y")
     _need(y, "y", (N, M), 4 if f32 else 2)
-    _here(x, expert_offsets, w, y, permuted_rows)
+    _here(x, w, y, whole=(expert_offsets, permuted_rows))
     _check("moe_grouped_matmul", lib().moe_grouped_matmul(
         _ptr(x), _ptr(permuted_rows), _ptr(expert_offsets), L, T, k, N, K, M, _ptr(w), _ptr(y),
         f32, _stream(stream)))
@@ -424,7 +429,7 @@ def grouped_matmul_dx(dy, expert_offsets, w, dx, stream=None):
     _need(w, "w", (L, M, K), 2)
     f32 = _out_fp32(dx, "dx")
     _need(dx, "dx", (N, K), 4 if f32 else 2)
-    _here(dy, expert_offsets, w, dx)
+    _here(dy, w, dx, whole=(expert_offsets,))
     _check("moe_grouped_matmul_dx", lib().moe_grouped_matmul_dx(
         _ptr(dy), _ptr(expert_offsets), L, N, K, M, _ptr(w), _ptr(dx), f32, _stream(stream)))
 
@@ -439,7 +444,7 @@ def grouped_matmul_dw(dy, x, expert_offsets, dw, permuted_rows=None, k=1, stream
     _need(x, "x", (T, K), 2)
     f32 = _out_fp32(dw, "dw")
     _need(dw, "dw", (L, M, K), 4 if f32 else 2)
-    _here(dy, x, expert_offsets, dw, permuted_rows)
+    _here(dy, x, dw, whole=(expert_offsets, permuted_rows))
     _check("moe_grouped_matmul_dw", lib().moe_grouped_matmul_dw(
         _ptr(dy), _ptr(x), _ptr(permuted_rows), _ptr(expert_offsets), L, T, k, N, K, M, _ptr(dw),
         f32, _stream(stream)))
@@ -483,7 +488,7 @@ def rms_norm_backward(dy, h, weight, eps, dx, dweight, ws, dresidual=None, strea
     _need(dweight, "dweight", (H,), 4)
     _need(dresidual, "dresidual", (T, H), 2, optional=True)
     nws = _need_ws(ws)
-    _here(dy, h, weight, dx, dweight, ws, dresidual)
+    _here(dy, h, weight, dx, dweight, dresidual, ws=ws)
     _check("moe_rms_norm_backward", lib().moe_rms_norm_backward(
         _ptr(dy), _ptr(h), _ptr(weight), eps, T, H, _ptr(dresidual), _ptr(dx), _ptr(dweight),
         _ptr(ws), nws, _stream(stream)))
@@ -522,7 +527,7 @@ def swiglu_quantize_mx(gu, codes, scales, rows=None, stream=None):
     bits = _mx_bits(codes, "codes", N, I2 // 2)
     _need(scales, "scales", (N, I2 // 64), 1)
     _need(rows, "rows", (1,), 4, optional=True)
-    _here(gu, codes, scales, rows)
+    _here(gu, codes, scales, whole=(rows,))
     _check("moe_swiglu_quantize_mx", lib().moe_swiglu_quantize_mx(
         _ptr(gu), f32, N, I2 // 2, _ptr(rows), bits, _ptr(codes), _ptr(scales), _stream(stream)))
 
@@ -553,7 +558,7 @@ def grouped_matmul_mx(xq, xs, expert_offsets, wq, ws, y, permuted_rows=None, k=1
     _need(ws, "ws", (L, M, K // 32), 1)
     f32 = _out_fp32(y, "y")
     _need(y, "y", (N, M), 4 if f32 else 2)
-    _here(xq, xs, expert_offsets, wq, ws, y, permuted_rows)
+    _here(xq, xs, wq, ws, y, whole=(expert_offsets, permuted_rows))
     _check("moe_grouped_matmul_mx", lib().moe_grouped_matmul_mx(
         _ptr(xq), _ptr(xs), bits, _ptr(permuted_rows), _ptr(expert_offsets), L, T, k, N, K, M,
         _ptr(wq), _ptr(ws), _ptr(y), f32, _stream(stream)))

@@ -204,3 +204,54 @@ def test_binding_refuses_types_of_the_same_size(monkeypatch, name):
     for call in calls:
         with pytest.raises(ValueError, match="type"):
             call()
+
+
+def test_binding_refuses_floats_for_whole_numbers_and_back(monkeypatch):
+    """float32 offsets, selections and row counts, int32 norm weights, values
+    and outputs: the same size, but their bits mean something else. A workspace
+    may have any type."""
+    import torch
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    def on(shape, dtype):
+        class On(F):
+            def get_device(self):
+                return 0
+        t = On(shape, dtype.itemsize)
+        t.dtype = dtype
+        return t
+
+    bf, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    T, K, M, L = 4, 64, 8, 2
+    x, y, w = on((T, K), bf), on((T, M), bf), on((L, M, K), bf)
+    off, rows = on((L + 1,), i32), on((T,), i32)
+    q, s, wq, ws = on((T, K), u8), on((T, 2), u8), on((L, M, K // 2), u8), on((L, M, 2), u8)
+    reached = []
+    monkeypatch.setattr(moe, "lib", lambda: reached.append(1) or (_ for _ in ()).throw(KeyError()))
+    calls = [
+        lambda o, r: moe.grouped_matmul(x, o, w, y, r),
+        lambda o, r: moe.grouped_matmul_dw(y, x, o, on((L, M, K), bf), r),
+        lambda o, r: moe.grouped_matmul_mx(q, s, o, wq, ws, y, r),
+    ]
+    bad = [lambda c=c: c(on((L + 1,), f32), rows) for c in calls]
+    bad += [lambda c=c: c(off, on((T,), f32)) for c in calls]
+    bad += [
+        lambda: moe.grouped_matmul_dx(y, on((L + 1,), f32), w, x),
+        lambda: moe.grouped_matmul(x, off, w, on((T, M), i32), rows),
+        lambda: moe.rms_norm(x, on((K,), i32), 1e-6, y=x),
+        lambda: moe.rms_norm_backward(x, x, on((K,), f32), 1e-6, x, on((K,), i32), None),
+        lambda: moe.quantize_mx(on((T, K), i32), q, s),
+        lambda: moe.dequantize_mx(q, s, on((T, K), i32)),
+        lambda: moe.swiglu_quantize_mx(on((T, 2 * K), bf), q, s, rows=on((1,), f32)),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError, match="type"):
+            call()
+        assert not reached, f"case {i} was let through"
+    good = [lambda c=c: c(off, rows) for c in calls]
+    good += [lambda: moe.rms_norm(x, on((K,), f32), 1e-6, y=on((T, K), torch.int16)),
+             lambda: moe.rms_norm_backward(x, x, on((K,), f32), 1e-6, x, on((K,), f32), off)]
+    for call in good:
+        with pytest.raises(KeyError):
+            call()
