@@ -39,8 +39,9 @@ def _compile(src):
 
 def _link(objs, out):
     tmp = out + ".tmp"
-    subprocess.check_call([HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC"] + objs +
-                          ["-o", tmp])
+    # a function that no object defines (a changed signature) fails here, not at the load
+    subprocess.check_call([HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-Wl,-z,defs"] +
+                          objs + ["-o", tmp])
     os.replace(tmp, out)
 
 

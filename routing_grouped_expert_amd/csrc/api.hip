@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "grouped.h"
+#include "operators.h"
 #include "plan.h"
 
 #include <cstdint>
@@ -37,24 +38,6 @@ bool ffn_plan_target(const void* x, const void* w1, const void* w2, const void* 
                      int L, int H, int I, bool f8, void* ws, PlanOut* po);
 hipError_t launch_combine(const float* eo, const int* e2p, const float* w, int T, int k, int H,
                           uint16_t* y, hipStream_t stream);
-hipError_t launch_grouped(Product p, const GroupedArgs& a, bool out_fp32, hipStream_t stream);
-hipError_t launch_rms_norm(const uint16_t* x, const uint16_t* res, const float* weight, float eps,
-                           int T, int H, uint16_t* h_out, uint16_t* y, uint8_t* yq, uint8_t* ys,
-                           hipStream_t s);
-size_t rms_norm_backward_workspace_bytes(int T, int H);
-hipError_t launch_rms_norm_backward(const uint16_t* dy, const uint16_t* h, const float* weight,
-                                    float eps, int T, int H, const uint16_t* dres, uint16_t* dx,
-                                    float* dweight, float* part, hipStream_t s);
-hipError_t launch_quantize_mx(const void* x, bool x_fp32, size_t n, int bits, uint8_t* codes,
-                              uint8_t* scales, hipStream_t s);
-hipError_t launch_swiglu_quantize_mx(const void* gu, bool gu_fp32, int N, int I, const int* rows,
-                                     int bits, uint8_t* codes, uint8_t* scales, hipStream_t s);
-hipError_t launch_dequantize_mx(const uint8_t* codes, const uint8_t* scales, size_t n, int bits,
-                                void* out, bool out_fp32, hipStream_t s);
-hipError_t launch_grouped_matmul_mx(const uint8_t* xq, const uint8_t* xs, int x_bits,
-                                    const int* rows, const int* off, int L, int T, int k, int N,
-                                    int K, int M, const uint8_t* wq, const uint8_t* ws, void* y,
-                                    bool y_fp32, hipStream_t s);
 }  // namespace moe
 
 namespace {

@@ -117,7 +117,6 @@ __device__ __forceinline__ DnTile dn_tile(const int* __restrict__ plan, int pmax
 
 // A buffer resource (four SGPRs) over `bytes` bytes from `base`: offsets at
 // or past `bytes` read zeros without a memory request.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x4 dn_rsrc4(const void* base, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
   return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, 0x00020000u};

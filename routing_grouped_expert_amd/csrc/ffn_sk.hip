@@ -453,7 +453,6 @@ __device__ __forceinline__ void up_mma(UpOps<RG, S>& r, f32x4 (&acc)[2 * RG], u1
 // its wave's range, codes 0..7 for the even step and 8..15 for the odd one.
 // The token fragments are loaded in the same K order, so the sum over K is
 // unchanged; codes are widened to bf16 exactly just before their MFMAs.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <int RG, int S>
 struct UpOps8 {
   static_assert(S % 2 == 0, "pairs of MFMA steps");

@@ -161,8 +161,6 @@ __device__ __forceinline__ int source_row(const Args& a, int n) {
   return a.rows ? token_of(a, a.rows[n]) : n;
 }
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 template <typename Out>
 __device__ __forceinline__ Out out_value(float v);
 template <>

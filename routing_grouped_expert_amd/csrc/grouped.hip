@@ -14,16 +14,12 @@
 // experts take 259 us.
 #include "mx_matmul.h"
 #include "lds_dma.h"
+#include "operators.h"
 
 #include <algorithm>
 #include <atomic>
 
 namespace moe {
-
-hipError_t launch_grouped_dense(Product p, const GroupedArgs& a, bool out_fp32, int lo, int blocks,
-                                hipStream_t stream);
-hipError_t launch_skinny(const MxArgs& a, int x_bits, bool y_fp32, int others, hipStream_t s);
-int skinny_rows();
 
 namespace {
 
@@ -177,7 +173,6 @@ bool fast_ok(const GroupedArgs& a) {
 
 }  // namespace
 
-// Compute units of the current device.
 int compute_units() {
   static std::atomic<int> cached[64];
   int dev = 0;

@@ -22,6 +22,7 @@
 // stores alone 0.41 ms and its loads 0.31.
 #include "grouped.h"
 #include "lds_dma.h"
+#include "operators.h"
 
 #include <algorithm>
 

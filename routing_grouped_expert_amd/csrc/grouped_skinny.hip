@@ -19,12 +19,11 @@
 // took 531 us (50 rows an expert, E2M1; the wide tiles 247) and 741 (bf16; 480).
 #include "lds_dma.h"
 #include "mx_matmul.h"
+#include "operators.h"
 
 #include <algorithm>
 
 namespace moe {
-
-int compute_units();
 
 namespace {
 

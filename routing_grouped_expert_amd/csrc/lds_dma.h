@@ -5,8 +5,6 @@
 
 namespace moe {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 // A buffer offset past every resource: the load reads zeros and makes no
 // memory request. Resources are kept shorter than this.
 constexpr uint32_t kPastEnd = 0xFFFFFFF0u;

@@ -16,6 +16,7 @@
 // weights' stream bounds it: 316 us, 3.8 TB/s, and 247 us, 4.9 TB/s.
 #include "lds_dma.h"
 #include "mx_matmul.h"
+#include "operators.h"
 
 namespace moe {
 

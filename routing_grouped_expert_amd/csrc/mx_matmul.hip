@@ -7,15 +7,9 @@
 // with few rows and the one for the others both run, and each passes over the
 // other's experts; the second is left out where no expert can have more.
 #include "mx_matmul.h"
+#include "operators.h"
 
 namespace moe {
-
-
-hipError_t launch_mx_dense(const MxArgs& a, int x_bits, bool y_fp32, int lo, int blocks,
-                           hipStream_t s);
-hipError_t launch_skinny(const MxArgs& a, int x_bits, bool y_fp32, int others, hipStream_t s);
-int skinny_rows();
-int compute_units();
 
 hipError_t launch_grouped_matmul_mx(const uint8_t* xq, const uint8_t* xs, int x_bits,
                                     const int* rows, const int* off, int L, int T, int k, int N,

@@ -7,15 +7,13 @@
 // values to 4 bits in 236 us, 5.0 TB/s (four pieces a lane at once and 8 blocks a
 // CU; 16 blocks 251 us), back in 250 us.
 #include "mx.h"
+#include "operators.h"
 
 #include <algorithm>
 
 namespace moe {
 
 namespace {
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
   const u16x8 u = *reinterpret_cast<const u16x8*>(p);

@@ -16,6 +16,7 @@
 // take a wave each, longer ones 8 values a thread where a block can (rows of
 // 4096: 26.5 us with 512 threads, 27.7 with 256 of two pieces).
 #include "mx.h"
+#include "operators.h"
 
 #include <algorithm>
 
@@ -23,11 +24,8 @@ namespace moe {
 
 namespace {
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
 // Eight fp32 to bf16.
 __device__ __forceinline__ u16x8 pack8(const float (&v)[8]) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   return __builtin_bit_cast(u16x8, u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
                                          pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
 }
