@@ -237,7 +237,8 @@ __global__ __launch_bounds__(WAVES * kWave) void skinny_kernel(MxArgs a, int mos
     wait_lds();  // read before the block's next meeting
     slot = slot == S_RING - 1 ? 0 : slot + 1;
     if (++cm.kc == nk) {
-      const bool vec = a.M % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0;
+      // (bf16 operands come here with whole 16-byte pieces of y only)
+      const bool vec = !MX || (a.M % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (j == 1 && !two) break;

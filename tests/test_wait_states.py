@@ -149,3 +149,17 @@ def test_asm_names_m0():
             if re.search(r"\bm0\s*,", code):
                 assert '"m0"' in rest or '"+{m0}"' in rest, f"{f}: {code.strip()}"
     assert found >= 4
+
+
+def test_no_stores_that_no_call_reaches(tmp_path):
+    """The few-row kernel stores single elements for microscaled operands only:
+    bf16 calls without whole 16-byte pieces of y go to another kernel."""
+    seen = 0
+    for name, ins in kernels(str(tmp_path)):
+        m = re.search(r"skinny_kernelILi(\d+)ELi\dE(\w)E", name)
+        if m:
+            single = "global_store_short" if m[2] == "t" else "global_store_dword"
+            stores = sum(op == single for _, op, _, _ in ins)
+            assert (stores > 0) == (m[1] != "16"), name
+            seen += 1
+    assert seen == 12
