@@ -12,11 +12,14 @@
 // the weights it multiplies; the rows of x are loaded once a block. The stages
 // run on across the block's tiles.
 //
-// Measured: bf16, 64 rows on 8 experts (K 4096, M 28672) 313 us, 6.0 TB/s (347
-// without the read-once policy on the weights); E2M1 weights, the same shape, 85
-// us, 5.9 TB/s; one token on 8 of 256 experts (K 7168, M 4096) 24 us. Above 32
-// rows the wide tiles are faster: an expert of 33 to 64 rows in two passes of 32
-// took 531 us (50 rows an expert, E2M1; the wide tiles 247) and 741 (bf16; 480).
+// Measured: bf16, 64 rows on 8 experts (K 4096, M 28672) 319 us, 5.9 TB/s (347
+// without the read-once policy on the weights); E2M1 weights, the same shape, 84
+// us with E2M1 rows, 6.0 TB/s, and 100 with E4M3 rows: 80 instructions more a
+// stage to split their fragments, and twice the matrix instructions (88 us without
+// either, mx_matmul.h says why they are there); one token on 8 of 256 experts (K
+// 7168, M 4096) 22 and 27 us. Above 32 rows the wide tiles are faster: an expert
+// of 33 to 64 rows in two passes of 32 took 741 us in bf16 (50 rows an expert; the
+// wide tiles 480).
 #include "lds_dma.h"
 #include "mx_matmul.h"
 #include "operators.h"
@@ -53,8 +56,11 @@ __device__ __forceinline__ int place(int q, int r) {
   return q ^ (r & (P - 1));
 }
 
+// (Launch bounds of 512 threads: with the 512 registers that fewer would leave a
+// lane, the compiler moves the accumulators to the other half of them and back in
+// every stage, 103 against 101 us.)
 template <int XB, int WAVES, typename Out>
-__global__ __launch_bounds__(WAVES * kWave) void skinny_kernel(MxArgs a, int most, int others) {
+__global__ __launch_bounds__(512) void skinny_kernel(MxArgs a, int most, int others) {
   using F = Format<XB>;
   constexpr bool MX = F::MX;
   constexpr int XPIECES = S_TOK * F::XROW / 1024;       // 1 KB pieces of a stage's x
@@ -72,8 +78,10 @@ __global__ __launch_bounds__(WAVES * kWave) void skinny_kernel(MxArgs a, int mos
   const int step = gridDim.x;
   const int KB = a.K / kMxBlock;
   // (with scales at least two stages, the second one of zeros where it has to
-  // be, so that a run of scales is never a single stage)
+  // be: two neighbouring runs are then four stages or more together, and the
+  // ring's five stages reach into three at most)
   const int nk = max(MX ? 2 : 1, (a.K + F::K - 1) / F::K);
+  const int whole = a.K / F::K;  // stages without a row's end
   const int per = (a.M + WAVES * S_ROWS - 1) / (WAVES * S_ROWS);
   const int wbytes = MX ? a.K / 2 : a.K * 2, xbytes = a.K * XB / 8;
 
@@ -141,21 +149,24 @@ __global__ __launch_bounds__(WAVES * kWave) void skinny_kernel(MxArgs a, int mos
   auto load = [&]() {
     const uint32_t mine = lds0 + sl * SLOT + wave * WAVE_BYTES, xto = lds0 + sl * SLOT + WAVES * WAVE_BYTES;
     const uint32_t aw = cl.kc * 128u, ax = cl.kc * (uint32_t)F::XROW;
-    uint32_t w_at[4], x_at[XN];
+    if (__builtin_expect(cl.kc < whole, 1)) {
+      dma16_run<true>(rw, mine, vw, aw);
+      dma16_run<false>(rx, xto + XN * wave * 1024u, vx, ax);
+    } else {  // pieces behind the rows' ends as zeros
+      uint32_t w_at[4], x_at[XN];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = 8 * j + (lane >> 3);
-      const bool in = (int)aw + place<8>(lane & 7, i) * 16 < wbytes;
-      w_at[j] = in ? vw[j] : kPastEnd;
-    }
-    dma16_run<true>(rw, mine, w_at, aw);
+      for (int j = 0; j < 4; ++j) {
+        const int i = 8 * j + (lane >> 3);
+        w_at[j] = (int)aw + place<8>(lane & 7, i) * 16 < wbytes ? vw[j] : kPastEnd;
+      }
+      dma16_run<true>(rw, mine, w_at, aw);
 #pragma unroll
-    for (int j = 0; j < XN; ++j) {
-      const int i = (XN * wave + j) * XROWS + lane / F::XP;
-      const bool in = (int)ax + place<F::XP>(lane % F::XP, i) * 16 < xbytes;
-      x_at[j] = in ? vx[j] : kPastEnd;
+      for (int j = 0; j < XN; ++j) {
+        const int i = (XN * wave + j) * XROWS + lane / F::XP;
+        x_at[j] = (int)ax + place<F::XP>(lane % F::XP, i) * 16 < xbytes ? vx[j] : kPastEnd;
+      }
+      dma16_run<false>(rx, xto + XN * wave * 1024u, x_at, ax);
     }
-    dma16_run<false>(rx, xto + XN * wave * 1024u, x_at, ax);
     if (MX && cl.kc % S_RUN == 0) {
       const uint32_t to = scales0 + run_l * 2048;
       dma16_bytes(rws, a.ws + (size_t)cl.expert * a.M * KB, ws_end, to,
@@ -216,22 +227,30 @@ __global__ __launch_bounds__(WAVES * kWave) void skinny_kernel(MxArgs a, int mos
     for (int j = 0; j < 2; ++j) {
       if (j == 0 || two) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s) {
+          if (MX) {
+            const i32x4 u = fx[j][s][0], v = fx[j][s][XB == 8 ? 1 : 0];
+            i32x8 x = {u[0], u[1], u[2], u[3], 0, 0, 0, 0}, small;
+            if (XB == 8) split_e4m3(i32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]}, &x, &small);
+            i32x8 w[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (MX) {
-              const i32x4 w = fw[i][s], x = fx[j][s][0], x1 = fx[j][s][XB == 8 ? 1 : 0];
-              acc[i][j] = mx_mfma<XB == 8 ? 8 : 4>(
-                  i32x8{w[0], w[1], w[2], w[3], 0, 0, 0, 0},
-                  XB == 8 ? i32x8{x[0], x[1], x[2], x[3], x1[0], x1[1], x1[2], x1[3]}
-                          : i32x8{x[0], x[1], x[2], x[3], 0, 0, 0, 0},
-                  acc[i][j], qw[i][s], qx[j][s]);
-            } else {
+            for (int i = 0; i < 2; ++i) {
+              const i32x4 f = fw[i][s];
+              w[i] = i32x8{f[0], f[1], f[2], f[3], 0, 0, 0, 0};
+              acc[i][j] = mx_mfma<XB == 8 ? 8 : 4>(w[i], x, acc[i][j], qw[i][s], qx[j][s]);
+            }
+            if (XB == 8)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                acc[i][j] = mx_mfma<8>(w[i], small, acc[i][j], qw[i][s], qx[j][s]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
               acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                   __builtin_bit_cast(bf16x8, fw[i][s]), __builtin_bit_cast(bf16x8, fx[j][s][0]),
                   acc[i][j], 0, 0, 0);
-            }
           }
+        }
       }
     }
     wait_lds();  // read before the block's next meeting

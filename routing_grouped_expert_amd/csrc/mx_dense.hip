@@ -11,9 +11,14 @@
 // of two to four stages: four at a time they were 40% of the load requests (share
 // of 77 experts at 32768 tokens, K 7168, M 4096: 1408 against 1289 us).
 //
-// That case is bound by the matrix cores (1.24 ms, 2.5 PFLOP/s of useful products;
-// torch's fp8 product of 8192^3 reaches 2.7). At 85 and 50 rows an expert the
-// weights' stream bounds it: 316 us, 3.8 TB/s, and 247 us, 4.9 TB/s.
+// With E4M3 rows that case is bound by the matrix cores, which multiply each
+// fragment in two parts (mx_matmul.h): 2.04 ms, 1.5 PFLOP/s of useful products and
+// 3.0 of the instruction's (torch's fp8 product of 8192^3 reaches 2.7); one part
+// took 1.24 ms. A fragment's parts are worked out among the matrix instructions of
+// the one before (2.07 to 2.20 ms in front of its own). E2M1 rows: 1.06 ms, 2.9
+// PFLOP/s, bound by the stages' LDS traffic beside them. At 85 and 50 rows an expert,
+// E4M3: 400 us, matrix instructions and the weights' stream (3.0 TB/s) alike, and
+// 270, 4.5 TB/s; E2M1: 300 and 238.
 #include "lds_dma.h"
 #include "mx_matmul.h"
 #include "operators.h"
@@ -30,8 +35,8 @@ constexpr int X_S = X_T * 16;  // bytes of the weights' scales for a run
 // Shape of a kind of tile: TC tokens. 256 for experts with many rows; 128 and 64
 // for the others, which the stream of their weights bounds: 128 leaves room for
 // more stages in flight, 64 for stages of 256 of the contraction, whole 128-byte
-// lines of the weights (77 experts, K 7168, M 4096, us with 64 / 128 tokens: 50
-// rows an expert 252 / 308, 85 in two passes 382 / 316).
+// lines of the weights (77 experts, K 7168, M 4096, E4M3 rows, us with 64 / 128
+// tokens: 50 rows an expert 265 / 386, 64 276 / 393, 85 in two passes 461 / 401).
 template <int XBITS, int TC>
 struct Shape {
   static constexpr int K = TC == 64 ? 256 : 128;   // contraction of a stage
@@ -297,6 +302,10 @@ __device__ __forceinline__ int mx_dense_tiles(const MxArgs& a, uint8_t* lds, int
           for (int c = 0; c < CG; ++c) qb[h][c] = out ? 127 : qb[h][c];
         }
       }
+      // the parts of an E4M3 fragment; those of the next one are worked out among the
+      // matrix instructions
+      i32x8 x = fb[0][0], small = {};
+      if (XBITS == kMxFp8) split_e4m3(fb[0][0], &x, &small);
       meet();
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(1);
@@ -304,10 +313,27 @@ __device__ __forceinline__ int mx_dense_tiles(const MxArgs& a, uint8_t* lds, int
       for (int c = 0; c < CG; ++c) {
         if (__builtin_expect(c < nv, 1)) {
 #pragma unroll
-          for (int h = 0; h < H; ++h)
+          for (int h = 0; h < H; ++h) {
+            constexpr int LAST = CG * H - 1;
+            const int n = min(c * H + h + 1, LAST);
+            i32x8 next = fb[n % H][n / H], next_small = {};
 #pragma unroll
             for (int r = 0; r < 8; ++r)
-              acc[r][c] = mx_mfma<XBITS>(fa[h][r], fb[h][c], acc[r][c], qa[h][r], qb[h][c]);
+              acc[r][c] = mx_mfma<XBITS>(fa[h][r], x, acc[r][c], qa[h][r], qb[h][c]);
+            if (XBITS == kMxFp8) {
+              if (c * H + h < LAST) split_e4m3(fb[n % H][n / H], &next, &next_small);
+#pragma unroll
+              for (int r = 0; r < 8; ++r)
+                acc[r][c] = mx_mfma<XBITS>(fa[h][r], small, acc[r][c], qa[h][r], qb[h][c]);
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {  // one matrix instruction, three others
+                __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(2, 3, 0);
+              }
+            }
+            x = next;
+            small = next_small;
+          }
         }
       }
       __builtin_amdgcn_s_setprio(0);
@@ -354,10 +380,10 @@ __device__ __forceinline__ int mx_dense_tiles(const MxArgs& a, uint8_t* lds, int
 }
 
 // The experts with more than lo rows. Those with at most kNarrowRows go to the
-// narrow tiles (77 experts, K 7168, M 4096, skewed counts, 50, 85, 125, 167 rows an
-// expert on average, us: limit 64: 339, 367, 414, 469; 128: 329, 351, 360, 453; 256:
-// 310, 387, 421, 502), numbered on behind the wide ones, so that the blocks share
-// all tiles evenly.
+// narrow tiles (77 experts, K 7168, M 4096, E4M3 rows, 85, 128, 160, 256 rows an
+// expert, us: limit 64: 568, 617, 619, 789; 128: 410, 448, 621, 813; 256: 392, 423,
+// 707, 804), numbered on behind the wide ones, so that the blocks share all tiles
+// evenly.
 template <int XBITS, typename Out>
 __global__ __launch_bounds__(X_THREADS, 1) void mx_dense_kernel(MxArgs a, int lo) {
   constexpr int B0 = Shape<XBITS, 256>::BYTES, B1 = Shape<XBITS, 128>::BYTES, B2 = Shape<XBITS, 64>::BYTES;

@@ -1,7 +1,8 @@
 // Grouped product on microscaled operands: y[n] = W[e] x[n] with MXFP4 weights
 // and MXFP8 or MXFP4 rows, on the scaled matrix instruction
-// v_mfma_scale_f32_16x16x128_f8f6f4 (products and sums in fp32, one scale per
-// 32 of the contraction and row applied by the instruction).
+// v_mfma_scale_f32_16x16x128_f8f6f4 (one scale per 32 of the contraction and row
+// applied by the instruction; exact products, fp32 sums, for which E4M3 rows go in
+// two parts: mx_matmul.h).
 //
 // Only the device knows how many rows an expert has, so the kernel for experts
 // with few rows and the one for the others both run, and each passes over the
