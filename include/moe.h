@@ -385,9 +385,9 @@ moe_status moe_grouped_matmul_dw(const uint16_t* dy, const uint16_t* x,
  *                 moe_quantize_mx of the unrounded y), both or neither; then
  *                 H must be a multiple of 32
  * residual_out and y may be x or residual themselves (in place); outputs must
- * not overlap otherwise. eps >= 0. The squares are fp32: a row with values
- * beyond 1e19 has an infinite mean and zeros in y. Limits: H <= 2^20,
- * T * H < 2^31.
+ * not overlap otherwise. eps >= 0. The squares are summed in fp32: a row whose
+ * squares add up to more than 3.4e38 (values of 1e19, or of 1e17 in long rows) has
+ * an infinite mean and zeros in y. Limits: H <= 2^20, T * H < 2^31.
  */
 moe_status moe_rms_norm(const uint16_t* x, const uint16_t* residual, const float* weight,
                         float eps, int32_t T, int32_t H, uint16_t* residual_out, uint16_t* y,
@@ -398,7 +398,9 @@ moe_status moe_rms_norm(const uint16_t* x, const uint16_t* residual, const float
  * row's 1 / sqrt(mean(h^2) + eps):
  *   dx = s (weight dy - h s^2 mean(weight dy h)) + dresidual
  *   dweight = sum over rows of dy h s   (a fixed order)
- * dx is the gradient of x and of residual alike.
+ * dx is the gradient of x and of residual alike. A row whose mean is infinite
+ * has s = 0: dx = dresidual and nothing in dweight, NaN where the mean of
+ * weight dy h is not finite either.
  *   dy, h       [T, H] bf16: the gradient of y, and moe_rms_norm's h
  *   dresidual   [T, H] bf16, the gradient arriving at residual_out, or NULL
  *   dx          [T, H] bf16 (output); may be dy or dresidual itself
@@ -427,14 +429,17 @@ moe_status moe_rms_norm_backward(const uint16_t* dy, const uint16_t* h, const fl
  *   codes   [R, K / 2] (bits 4) or [R, K] (bits 8) (output)
  *   scales  [R, K / 32] (output)
  * moe_swiglu_quantize_mx -- the same of a = silu(gu[r, 0:I]) * gu[r, I:2I]
- * (a in fp32), the step between an expert's two products.
+ * (a in fp32; gates below -88.7, whose exponential overflows, give -0), the step
+ * between an expert's two products.
  *   gu      [N, 2I] bf16 or fp32; I a multiple of 32
  *   num_rows  DEVICE pointer to the number of rows to take (cut to [0, N];
  *           rows behind are neither read nor written), for instance
  *           expert_offsets + num_local; NULL: N
  *   codes, scales  as above with R = N, K = I
  * moe_dequantize_mx -- out[r, c] = value(code) * 2^(scale code - 127), exact
- * in fp32 and rounded once in bf16; NaN for scale code 255.
+ * in fp32 (infinity past its largest value, which E4M3 reaches under scale codes
+ * from 247 on and E2M1 from 253 on) and rounded once in bf16; NaN for scale code
+ * 255.
  *
  * Limits: R * K, N * 2I < 2^34. Pointers must be 16-byte aligned except
  * scales. R = 0 or N = 0 launches nothing.

@@ -11,7 +11,8 @@
 // matrix; a stage's elements are on their way to registers while the one before
 // it is multiplied (a training step at K 243, M 558 and 180 rows: 34 us, 96
 // without). Bound by the loads' latency and number: K 777, M 951, 4000 rows of 16
-// experts take 259 us.
+// experts take 53 us forward, 66 dx, 63 dw, and 133 dw by selections, which are
+// read and divided for every element of x (the bytes of each take 8 us).
 #include "mx_matmul.h"
 #include "lds_dma.h"
 #include "operators.h"

@@ -4,21 +4,25 @@
 // D[r, c] = sum over kk of A[r, kk] B[c, kk] (grouped.h says what r, c and kk
 // are in each product). An operand is "rows" when kk is contiguous in memory
 // (W and x in the forward, dy in dx) and "columns" when r or c is (W in dx, x
-// and dy in dw). Both go to LDS as they lie in memory, 32 of kk a stage, by
+// and dy in dw). Both go to LDS as they lie in memory, 32 or 64 of kk a stage, by
 // loads that write LDS directly; the fragments of a column operand are read
 // with the transposing LDS read (ds_read_b64_tr_b16), so no product needs a
 // transposed copy of anything.
 //
-// What bounds it. Many rows an expert (8 experts of about 2048 rows, K 4096, M
-// 14336): forward 1.55, dx 1.98, dw 2.03 ms in a training step (1.24, 0.97, 0.95
-// PFLOP/s; torch's single products of one expert's size reach 1.42, 1.14, 1.02), dx
-// with 4.5 rounds of tiles in five (rows in whole tiles, by itself: 1.50 ms).
-// The matrix instructions alone take 1.43 ms and the loads alone 1.44 ms: a tile
-// edge of 256 asks for 16 GB from the L2s, a fifth of it missing there, and they
-// deliver 11 TB/s of such a stream whatever the number of loads in flight; the
-// clock is 1.9 GHz under this load. Tens of rows (77 experts of 85, K 7168, M
-// 2048): forward 0.46, dx 0.46 ms, 4.9 TB/s of weights (forward: 2.4 rounds of
-// tiles in three; 5.4 TB/s where they fill theirs); dw 0.61 ms, its 2.26 GB of
+// What bounds it. Many rows an expert (8 experts of 2048 rows, K 4096, M 14336):
+// forward 1.54, dx 1.53, dw 1.79 ms (1.25, 1.26, 1.08 PFLOP/s; torch's single
+// products of one expert's size reach 1.42, 1.14, 1.02). Of the forward the matrix
+// instructions alone take 1.43 ms and the loads alone 1.44 ms: a tile edge of 256
+// asks for 16 GB from the L2s, a fifth of it missing there, and they deliver 11 TB/s
+// of such a stream whatever the number of loads in flight; the clock is 1.9 GHz
+// under this load. Routed counts end experts in parts of tiles: dx takes 1.79 ms
+// with 69 tiles of rows for 64 (five rounds of tiles for 4.3). dw has the same
+// stream, but ends a tile after 64 stages instead of 128, 4 to 5 us each time with
+// its next loads behind the stores (1.65 ms for experts of 4096 rows and M 7168,
+// 1.72 at 2048 and 14336, 1.85 at 1024 and 28672, all without selections), and its
+// selections take 0.08 ms. The three one after the other take 5.5 ms, 0.4 more than
+// by themselves, most of it in dw (2.0). Tens of rows (77 experts of 85, K 7168, M
+// 2048): forward 0.44, dx 0.45 ms, 5.1 TB/s of weights; dw 0.61 ms, its 2.26 GB of
 // stores alone 0.41 ms and its loads 0.31.
 #include "grouped.h"
 #include "lds_dma.h"
@@ -38,15 +42,16 @@ constexpr int D_THREADS = 512;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// ---- the two LDS layouts of an operand's stage (16 KB, written in 16 pieces
-// of 1 KB by the direct loads: lane i of piece b fills bytes 1024 b + 16 i)
+// ---- the two LDS layouts of an operand's stage (written in pieces of 1 KB by the
+// direct loads: lane i of piece b fills bytes 1024 b + 16 i)
 //
-// rows:    256 rows of 64 bytes; the 16 bytes q of row r sit at slot
-//          q ^ ((r >> 1) & 3), so a fragment read (16 rows, one 16-byte piece
-//          each) meets no bank twice.
-// columns: 32 rows (kk) of 512 bytes; in units of 32 bytes, unit u of row kk
-//          sits at u ^ f(kk), f(kk) = (kk & 3) | ((kk >> 3) & 1) << 2, so the
-//          8 rows that half a wave reads together lie in 8 different units.
+// rows:    256 rows (128 of B in the narrow tiles) of a stage's K values: 64 bytes,
+//          the 16 bytes q of row r at slot q ^ ((r >> 1) & 3), or 128 bytes, at
+//          q ^ (r & 7), so a fragment read (16 rows, one 16-byte piece each) meets
+//          no bank twice.
+// columns: the stage's K rows (kk) of 512 bytes; in units of 32 bytes, unit u of
+//          row kk sits at u ^ f(kk), f(kk) = (kk & 3) | ((kk >> 3) & 1) << 2, so
+//          the 8 rows that half a wave reads together lie in 8 different units.
 
 // Place of 16-byte piece q of row r in the rows layout, or the piece at place q.
 template <int K>
@@ -161,7 +166,7 @@ struct Work {
   }
 };
 
-// A stage of the block's work: 32 of the contraction of a tile.
+// A stage of the block's work: Shape<TC>::K of the contraction of a tile.
 template <Product P, int TC>
 struct Cursor {
   Work<P, TC>& work;
@@ -183,7 +188,7 @@ struct Cursor {
   }
 };
 
-// The wave's loads: pieces 2 w and 2 w + 1 of A's stage, and BN pieces of B's.
+// The wave's loads: AN pieces of A's stage, from AN w on, and BN of B's.
 // PICKS: dw whose x rows go by selections.
 template <Product P, bool PICKS, int TC>
 struct Loads {
@@ -284,17 +289,20 @@ struct Loads {
 // Eight waves: 128 of r x CG groups of 16 of c each (every fourth group of the
 // tile's, so that the waves share a partly filled tile evenly). A stage is two
 // parts with a block barrier after each: reading its fragments from LDS (and
-// starting the loads of the stage S - 1 ahead, S the number of slots), and its 8
-// CG matrix instructions. Waves 4-7 run one part behind waves 0-3 (they meet one
+// starting the loads of the stage S - 1 ahead, S the number of slots), and its
+// matrix instructions. Waves 4-7 run one part behind waves 0-3 (they meet one
 // barrier more at the start), and waves w and w + 4 share a SIMD: while one of
 // them multiplies the other reads.
 //
 // Stage i + S goes into the slot of stage i. Count the parts by the barriers
 // that end them: waves 0-3 read stage i in part 2 i, waves 4-7 in part 2 i + 1,
-// and wait for what they read before the barrier. The first load into the slot
-// is issued in part 2 i + 2. It is waited for, with S - 3 stages of loads still
-// in flight, in part 2 (i + S) - 2 or one later, and first read in part
-// 2 (i + S).
+// and wait for what they read before the barrier. The first load into the slot is
+// issued in the reading part of stage i + 1, by waves 0-3 in part 2 i + 2. It is
+// waited for in the reading part of stage i + S - 1, part 2 (i + S) - 2 or one
+// later, and first read in part 2 (i + S). Behind the stage waited for, loads of
+// AHEAD stages are then in flight: S - 3 where that part's own loads are issued
+// behind the wait (256 columns: stages i + S + 1 .. i + 2 S - 3), S - 2 where they
+// are issued in front of it (EARLY, 128 columns: one stage more).
 //
 // dw's x rows go by selections, which have to be there when the loads are
 // issued: they are loaded three stages further ahead, each wave its own copy,
@@ -403,9 +411,10 @@ __device__ __forceinline__ int dense_tiles(const GroupedArgs& a, uint8_t* lds, i
   };
   clear();
   uint32_t from = lds0;  // slot of the stage being multiplied
-  // A whole tile's stores are STORES instructions. In the S - 2 stages behind
-  // them the loads waited for were issued before the stores: the stores, and
-  // the S - 3 stages of loads issued since those, may still be in flight.
+  // A whole tile's stores are STORES instructions. Stage t behind them waits for
+  // stage t + 1, whose loads were issued S - 1 stages before that: for t up to S - 2
+  // in front of the stores, which may then still be in flight, as the AHEAD stages
+  // of loads behind those waited for may.
   constexpr int STORES = kTileStores<Out> * CG / 4;
   constexpr int FLIGHT = S::AHEAD * (S::LOADS + (PICKS ? 1 : 0));
   int after_stores = 0;

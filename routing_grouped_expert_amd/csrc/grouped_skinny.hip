@@ -230,8 +230,12 @@ __global__ __launch_bounds__(512) void skinny_kernel(MxArgs a, int most, int oth
         for (int s = 0; s < 2; ++s) {
           if (MX) {
             const i32x4 u = fx[j][s][0], v = fx[j][s][XB == 8 ? 1 : 0];
-            i32x8 x = {u[0], u[1], u[2], u[3], 0, 0, 0, 0}, small;
-            if (XB == 8) split_e4m3(i32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]}, &x, &small);
+            i32x8 x = {u[0], u[1], u[2], u[3], 0, 0, 0, 0}, small = x;
+            if (XB == 8) {
+              small = i32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+              x = large_e4m3(small);
+              small ^= x;
+            }
             i32x8 w[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {

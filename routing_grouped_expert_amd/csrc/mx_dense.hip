@@ -12,13 +12,12 @@
 // of 77 experts at 32768 tokens, K 7168, M 4096: 1408 against 1289 us).
 //
 // With E4M3 rows that case is bound by the matrix cores, which multiply each
-// fragment in two parts (mx_matmul.h): 2.04 ms, 1.5 PFLOP/s of useful products and
-// 3.0 of the instruction's (torch's fp8 product of 8192^3 reaches 2.7); one part
-// took 1.24 ms. A fragment's parts are worked out among the matrix instructions of
-// the one before (2.07 to 2.20 ms in front of its own). E2M1 rows: 1.06 ms, 2.9
-// PFLOP/s, bound by the stages' LDS traffic beside them. At 85 and 50 rows an expert,
-// E4M3: 400 us, matrix instructions and the weights' stream (3.0 TB/s) alike, and
-// 270, 4.5 TB/s; E2M1: 300 and 238.
+// fragment in two parts (mx_matmul.h): 1.89 ms, 1.65 PFLOP/s of useful products and
+// 3.3 of the instruction's (torch's fp8 product of 8192^3 reaches 2.7), 2.1 to 2.2 ms
+// for routed counts; one part took 1.2 and 1.3. E2M1 rows: 1.06 ms, 2.9 PFLOP/s,
+// bound by the stages' LDS traffic beside them. At 85 and 50 rows an expert, E4M3:
+// 390 us, matrix instructions and the weights' stream (3.1 TB/s) alike, and 270, 4.5
+// TB/s; E2M1: 300 and 238.
 #include "lds_dma.h"
 #include "mx_matmul.h"
 #include "operators.h"
@@ -96,6 +95,20 @@ struct Rows {
     dma16_run<false>(rs, to + N * wave * 1024u, from, (uint32_t)at);
   }
 };
+
+// TIMES times in the compiler's order: MATRIX matrix instructions, VECTOR others.
+// An E4M3 fragment has 16 and 40 (8 for its small part, 32 for the next one's large
+// part), for which the matrix cores would stand still if they came together (683
+// rows an expert 1979 us in the compiler's own order; 1964 one by one; 1929 with the
+// first four by themselves. Narrower tiles, 50 rows: 271 one by one, 279).
+template <int MATRIX, int VECTOR, int TIMES>
+__device__ __forceinline__ void mx_order() {
+#pragma unroll
+  for (int r = 0; r < TIMES; ++r) {
+    __builtin_amdgcn_sched_group_barrier(8, MATRIX, 0);
+    __builtin_amdgcn_sched_group_barrier(2, VECTOR, 0);
+  }
+}
 
 // Tiles tm, tm + gridDim.x, .. of the experts with more than lo and at most hi
 // rows. Returns by how much the next of these numbers is past the last tile.
@@ -302,10 +315,9 @@ __device__ __forceinline__ int mx_dense_tiles(const MxArgs& a, uint8_t* lds, int
           for (int c = 0; c < CG; ++c) qb[h][c] = out ? 127 : qb[h][c];
         }
       }
-      // the parts of an E4M3 fragment; those of the next one are worked out among the
-      // matrix instructions
-      i32x8 x = fb[0][0], small = {};
-      if (XBITS == kMxFp8) split_e4m3(fb[0][0], &x, &small);
+      // the large part of an E4M3 fragment; the small one is made where the fragment
+      // was while the large one is multiplied, the next large one while the small one is
+      i32x8 x = XBITS == kMxFp8 ? large_e4m3(fb[0][0]) : fb[0][0];
       meet();
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(1);
@@ -316,25 +328,25 @@ __device__ __forceinline__ int mx_dense_tiles(const MxArgs& a, uint8_t* lds, int
           for (int h = 0; h < H; ++h) {
             constexpr int LAST = CG * H - 1;
             const int n = min(c * H + h + 1, LAST);
-            i32x8 next = fb[n % H][n / H], next_small = {};
 #pragma unroll
             for (int r = 0; r < 8; ++r)
               acc[r][c] = mx_mfma<XBITS>(fa[h][r], x, acc[r][c], qa[h][r], qb[h][c]);
             if (XBITS == kMxFp8) {
-              if (c * H + h < LAST) split_e4m3(fb[n % H][n / H], &next, &next_small);
+              fb[h][c] ^= x;
+              if (c * H + h < LAST) x = large_e4m3(fb[n % H][n / H]);
 #pragma unroll
               for (int r = 0; r < 8; ++r)
-                acc[r][c] = mx_mfma<XBITS>(fa[h][r], small, acc[r][c], qa[h][r], qb[h][c]);
-              // one matrix instruction, three others (128 rows an expert: 474 -> 427 us;
-              // 256 tokens in this order take registers out to memory in every stage)
-#pragma unroll
-              for (int r = 0; r < (TC == 256 ? 0 : 16); ++r) {
-                __builtin_amdgcn_sched_group_barrier(8, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(2, 3, 0);
+                acc[r][c] = mx_mfma<XBITS>(fa[h][r], fb[h][c], acc[r][c], qa[h][r], qb[h][c]);
+              if (TC == 256) {
+                mx_order<5, 2, 1>();
+                mx_order<1, 2, 3>();
+              } else {
+                mx_order<1, 1, 8>();
               }
+              mx_order<1, 4, 8>();
+            } else {
+              x = fb[n % H][n / H];
             }
-            x = next;
-            small = next_small;
           }
         }
       }

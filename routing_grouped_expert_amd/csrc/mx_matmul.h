@@ -44,18 +44,19 @@ __device__ __forceinline__ f32x4 mx_mfma(const i32x8& w, const i32x8& x, const f
 // 2^-10 on, above 2^(0 + 2 - 13): nothing is cut, and the sums are those of fp32.
 // It costs the matrix instructions twice (times at the kernels). E2M1 rows need
 // none of it: their products lie within 8 places.
-__device__ __forceinline__ void split_e4m3(const i32x8& x, i32x8* large, i32x8* small) {
+// The first part; what it leaves of x (x ^ it) is the second.
+__device__ __forceinline__ i32x8 large_e4m3(const i32x8& x) {
+  i32x8 r = x;
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t v = (uint32_t)x[i];
     // 0xFF in the bytes with bit 6: the selectors from 8 on fill a byte with bit 15 or
     // 31 of the second operand, or of the first
-    const uint32_t m = __builtin_amdgcn_perm(v << 9, v << 1, 0x090B080Au);
-    (*large)[i] = (int)(v & m);
-    (*small)[i] = (int)(v & ~m);
+    r[i] = (int)(v & __builtin_amdgcn_perm(v << 9, v << 1, 0x090B080Au));
   }
 #endif
+  return r;
 }
 
 }  // namespace moe
