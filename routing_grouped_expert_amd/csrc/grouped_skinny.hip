@@ -299,8 +299,8 @@ template <int XB>
 void launch_format(const MxArgs& a, bool y_fp32, int others, hipStream_t s) {
   const int cus = compute_units();
   // At most so many tiles of four waves; where they would not reach every CU,
-  // one wave a block. (K 7168, 128 / 256 tiles of four waves, us: one wave bf16 44
-  // / 86, E2M1 20 / 38; four waves 57 / 73, 22 / 23.)
+  // one wave a block. (K 7168, 128 / 256 tiles of four waves, us: one wave bf16 42
+  // / 78, E4M3 rows 25 / 45, E2M1 17 / 30; four waves 62 / 71, 26 / 27, 21 / 23.)
   const long tiles = ((long)a.N / S_TOK + std::min(a.L, a.N)) * ((a.M + 127) / 128);
   const bool wide = tiles >= cus;
   if (wide) {
@@ -320,9 +320,10 @@ int skinny_rows() { return S_TOK; }
 // x_bits 4, 8: microscaled operands; 16: bf16 (wq and xq then hold bf16). others:
 // blocks of the launch that follows, for the experts with more rows, or 0; where
 // it can take these experts along in its last round of tiles, it does, and this
-// one ends. (77 experts, one of them with few rows, K 7168, M 2048: 553 -> 506
-// us; 3 of 8, M 14336: bf16 431 -> 349, E2M1 176 -> 143. Where they make a
-// further round, 26 of 77: taken along 488, as here 480; E2M1 206 and 198.)
+// one ends. (77 experts of 85 rows, one with 20, K 7168, M 2048: bf16 491 -> 445 us,
+// E4M3 rows 250 -> 223; 3 of 8 with 20 rows, 5 with 300, K 4096, M 14336: 355 -> 300,
+// 246 -> 213. Where they make a further round, 26 of 77: taken along 434 and 189, as
+// here 430 and 214.)
 hipError_t launch_skinny(const MxArgs& a, int x_bits, bool y_fp32, int others, hipStream_t s) {
   if (x_bits == 4) launch_format<4>(a, y_fp32, others, s);
   if (x_bits == 8) launch_format<8>(a, y_fp32, others, s);

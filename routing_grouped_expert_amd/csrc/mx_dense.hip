@@ -35,7 +35,7 @@ constexpr int X_S = X_T * 16;  // bytes of the weights' scales for a run
 // for the others, which the stream of their weights bounds: 128 leaves room for
 // more stages in flight, 64 for stages of 256 of the contraction, whole 128-byte
 // lines of the weights (77 experts, K 7168, M 4096, E4M3 rows, us with 64 / 128
-// tokens: 50 rows an expert 265 / 386, 64 276 / 393, 85 in two passes 461 / 401).
+// tokens: 50 rows an expert 282 / 382, 64 282 / 380, 85 in two passes 457 / 399).
 template <int XBITS, int TC>
 struct Shape {
   static constexpr int K = TC == 64 ? 256 : 128;   // contraction of a stage
@@ -394,10 +394,10 @@ __device__ __forceinline__ int mx_dense_tiles(const MxArgs& a, uint8_t* lds, int
 }
 
 // The experts with more than lo rows. Those with at most kNarrowRows go to the
-// narrow tiles (77 experts, K 7168, M 4096, E4M3 rows, 85, 128, 160, 256 rows an
-// expert, us: limit 64: 568, 617, 619, 789; 128: 410, 448, 621, 813; 256: 392, 423,
-// 707, 804), numbered on behind the wide ones, so that the blocks share all tiles
-// evenly.
+// narrow tiles (77 experts, K 7168, M 4096, E4M3 rows, skewed counts, 50, 85, 125,
+// 167 rows an expert on average, us: limit 64: 372, 427, 610, 688; 128: 362, 379,
+// 483, 657; 256: 333, 434, 564, 697), numbered on behind the wide ones, so that the
+// blocks share all tiles evenly.
 template <int XBITS, typename Out>
 __global__ __launch_bounds__(X_THREADS, 1) void mx_dense_kernel(MxArgs a, int lo) {
   constexpr int B0 = Shape<XBITS, 256>::BYTES, B1 = Shape<XBITS, 128>::BYTES, B2 = Shape<XBITS, 64>::BYTES;
