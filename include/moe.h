@@ -442,7 +442,7 @@ moe_status moe_rms_norm_backward(const uint16_t* dy, const uint16_t* h, const fl
  * 255.
  *
  * Limits: R * K, N * 2I < 2^34. Pointers must be 16-byte aligned except
- * scales. R = 0 or N = 0 launches nothing.
+ * scales. Outputs must not overlap inputs. R = 0 or N = 0 launches nothing.
  */
 moe_status moe_quantize_mx(const void* x, int32_t x_fp32, int32_t R, int32_t K, int32_t bits,
                            uint8_t* codes, uint8_t* scales, void* stream);

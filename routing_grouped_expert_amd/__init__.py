@@ -548,7 +548,8 @@ def dequantize_mx(codes, scales, out, stream=None):
 def grouped_matmul_mx(xq, xs, expert_offsets, wq, ws, y, permuted_rows=None, k=1, stream=None):
     """moe_grouped_matmul_mx: grouped_matmul of MXFP8 rows (xq [T, K]) or MXFP4
     rows (xq [T, K // 2]), scales xs [T, K // 32], with MXFP4 weights (wq
-    [L, M, K // 2], ws [L, M, K // 32]); y [N, M] bf16 or fp32."""
+    [L, M, K // 2], ws [L, M, K // 32]); y [N, M] bf16 or fp32. Exact products,
+    fp32 sums, for which MXFP8 rows are multiplied in two parts."""
     N, M = _dims(y, "y", 2)
     T, _, L = _grouped_rows(xq, expert_offsets, permuted_rows, k, N)
     K = 2 * _dims(wq, "wq", 3)[2]

@@ -163,7 +163,8 @@ __device__ __forceinline__ int mx_dense_tiles(const MxArgs& a, uint8_t* lds, int
   bool edge;           // a lane's scales may end the array
   auto tile_loads = [&]() {
     // (a copy that hides its value: what is computed from it is not kept in
-    // registers, which the stage loop has none left of)
+    // registers, which the stage loop has none left of; with E4M3 rows one or two
+    // values are still stored to memory and read back here)
     int lane = threadIdx.x % kWave;
     asm volatile("" : "+v"(lane));
     const size_t left = (size_t)(a.L - cl.expert) * a.M;  // weight rows to the end
